@@ -397,10 +397,11 @@ __device__ __forceinline__ void extremes(const uint4* r, float& top, float& leas
   least = min_nan(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u));
 }
 
-// Whether x log2(e) of every element is an ordinary number: a segment whose
-// maximum and the thread's minimum lie within this takes the short form of its
-// exponentials.
-constexpr float kOrdinary = 1e30f;
+// The short form of a thread's exponentials: its smallest element is at least
+// kLeast, so that x log2(e) is finite, and the segment's maximum is less than
+// kMostShort away from 0.  c = m log2(e) is then below 2^21 and its rounding d at
+// most 2^-4; from about 2^30 on, 2^d and 2^-d would overflow.
+constexpr float kLeast = -1e30f, kMostShort = 1048576.f;
 
 constexpr int kStages = 2;                              // segments on their way or in use
 constexpr int kBlocksPerSm = 3;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) m = max_nan(m, wm[parity][w]);
       float s = 0.f, t = 0.f;
-      if (least > -kOrdinary && m < kOrdinary) {
+      if (least > kLeast && fabsf(m) < kMostShort) {
         // e = 2^(x log2 e - c) with c the rounded m log2 e; the rounding d of c
         // is a factor 2^d of every e, taken out at the end
         const float c = m * kLog2e, d = fmaf(m, kLog2e, -c);
