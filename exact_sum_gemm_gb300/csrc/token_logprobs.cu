@@ -48,8 +48,9 @@ typedef __nv_bfloat16 bf16;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVpt = 8;                                 // vectors of a segment per thread
-// Stands for x - m where that is -inf: exp gives 0, and 0 times it is 0.
-constexpr float kLowest = -1e30f;
+// Stands for x - m where that is less, down to -inf: exp gives 0 all the same,
+// and 0 times it, or times its product with a gradient, is 0.
+constexpr float kLowest = -1000.f;
 
 template <typename T>
 constexpr int segment_elems() { return kThreads * kVpt * Elem<T>::kVec; }

@@ -1,4 +1,6 @@
-"""Token log probabilities of large finite logits, against the 64-bit definition."""
+"""Token log probabilities of large finite logits and large gradients, against the 64-bit definition."""
+import math
+
 import pytest
 import torch
 
@@ -59,3 +61,19 @@ def test_logits_around_a_large_level(level, dt):
     """Every logit next to a level whose rounding is felt: differences of a few spacings."""
     x, t, g, h = make(6, dt, seed=1)
     check((x.to(F32) + level).to(dt), t, g, h)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_large_entropy_gradients(dt):
+    """-inf logits have no gradient, however large the gradient of the entropy is."""
+    x, t, g, h = make(4, dt, seed=2)
+    x[0, ::3] = -math.inf
+    x[1, 5:] = torch.finfo(dt).min
+    x[2, 100:] = -1e10
+    h = torch.full_like(h, 1e12)
+    t[0], t[1], t[2] = 1, 2, 3
+    lp, entropy, stats, _, _ = dg.det_token_logprobs_forward(x, t)
+    dx = dg.det_token_logprobs_backward(g, h, x, t, entropy, stats)
+    assert dx.isfinite().all()
+    assert not dx[0, ::3].any() and not dx[1, 5:].any() and not dx[2, 100:].any()
+    assert_within(dx, *token_logprobs(x, t, 0, g, h)["dlogits"], "dlogits")
