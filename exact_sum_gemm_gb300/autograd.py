@@ -1,11 +1,13 @@
 """Layer norm, attention and token log probabilities as differentiable functions.
 
 With DetLinear they make a decoder's training step whose every forward and
-backward operation repeats bit for bit.
+backward operation repeats bit for bit.  There are no second derivatives: asking
+for one raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .training import (det_attention_backward, det_attention_forward, det_layer_norm_backward,
                        det_layer_norm_forward, det_token_logprobs_backward,
@@ -20,6 +22,7 @@ class _LayerNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, mean, rstd, weight, bias = ctx.saved_tensors
         dx, dweight, dbias = det_layer_norm_backward(
@@ -63,6 +66,7 @@ class _AttentionFn(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, k_lengths = ctx.saved_tensors
         need_q, need_k, need_v = ctx.needs_input_grad[:3]
@@ -85,6 +89,7 @@ class _TokenLogprobsFn(torch.autograd.Function):
         return logprobs, entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dlogprobs, dentropy):
         if dlogprobs is None and dentropy is None:
             return None, None

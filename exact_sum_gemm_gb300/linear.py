@@ -11,10 +11,13 @@ With ``k_shards = s > 1`` every GEMM is instead computed as s K-shard
 partials (``cuts`` picks the cut points, equal shards by default), one combine
 and one finalize; the page's "Method" section says this gives identical
 bytes, and with ``bias=True`` the bias is one more partial of K = 1.
+
+The backward pass has no derivative of its own: asking for one raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (det_combine, det_finalize, det_gemm_partial, det_linear_bias_grad,
                det_linear_dgrad, det_linear_forward, det_linear_forward_bias, det_linear_wgrad)
@@ -54,6 +57,7 @@ class _DetLinearFn(torch.autograd.Function):
         return det_linear_forward(x.contiguous(), weight.contiguous())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight = ctx.saved_tensors
         dy = dy.contiguous().to(torch.float32)
