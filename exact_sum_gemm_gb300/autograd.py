@@ -103,6 +103,10 @@ def det_token_logprobs(logits, tokens):
     A negative token marks a place without one: its log probability is 0 and
     has no gradient.
     """
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError(f"logits must be [..., vocab], got {tuple(logits.shape)}")
+    if tokens.shape != logits.shape[:-1]:
+        raise ValueError(f"tokens must have shape {tuple(logits.shape[:-1])}, got {tuple(tokens.shape)}")
     vocab = logits.shape[-1]
     logprobs, entropy = _TokenLogprobsFn.apply(logits.reshape(-1, vocab), tokens.reshape(-1))
     return logprobs.reshape(tokens.shape), entropy.reshape(tokens.shape)
