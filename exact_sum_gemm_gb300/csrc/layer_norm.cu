@@ -260,6 +260,9 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide_kernel(Layer
   }
 }
 
+// Rows that kTpr threads share backward are wider than this (see the dispatch).
+constexpr int narrowest(int tpr) { return tpr == 32 ? 0 : tpr == 128 ? 512 : 8 * tpr; }
+
 // Block `block` of `blocks` takes rows block, block + blocks, ... (times
 // kThreads / kTpr rows at once), writes their dx and, with kSums, keeps its own
 // sums of dy xhat and dy, written at the end as one row of the partial sums
@@ -269,6 +272,7 @@ template <typename T, typename TW, int kThreads, int kTpr, int kDepth, bool kSum
 __device__ __forceinline__ void backward_rows(const LayerNormGradArgs& a, int block, int blocks) {
   constexpr int V = Elem<T>::kVec, kVpt = kElems / V;
   constexpr int kRows = kThreads / kTpr;
+  constexpr int kWhole = narrowest(kTpr) / (kTpr * V);  // a thread's first vectors, never past the row's end
   // 1024 threads have 64 registers each: no room for a row beside the sums, so
   // that it is read from the ring again (16384 columns: 175 us with spills)
   constexpr bool kAgain = kThreads == 1024;
@@ -318,17 +322,25 @@ __device__ __forceinline__ void backward_rows(const LayerNormGradArgs& a, int bl
     float s1 = 0.f, s2 = 0.f;
     // xhat and g = dy w of vector i
     auto read = [&](int i, float (&xh)[V], float (&dy)[V], float (&g)[V]) {
+      // columns past the row's end have dy = 0 and xhat = 0 ((0 - m) rs may be infinite)
+      const int left = W - (lane + i * kTpr) * V;       // elements of the vector within the row
+      const bool past = kPlain && i >= kWhole && left <= 0;
       uint4 rx = v[i * kThreads], rd = v[(kVpt + i) * kThreads];
-      if (kPlain && (lane + i * kTpr) * V >= W) rx = rd = make_uint4(0, 0, 0, 0);
+      if (past) rx = rd = make_uint4(0, 0, 0, 0);
+      const float mean = past ? 0.f : m;
       Elem<T>::unpack(rx, xh);
       Elem<T>::unpack(rd, dy);
       float w[V];
       if (a.weight) weight.get(i, lane + i * kTpr, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        // (columns past the row's end have dy = 0)
-        xh[e] = (xh[e] - m) * rs;
+        xh[e] = (xh[e] - mean) * rs;
         g[e] = a.weight ? dy[e] * w[e] : dy[e];
+      }
+      if (!kPlain && i >= kWhole && left < V) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (e >= left) xh[e] = 0.f;
       }
     };
     float xh[kVpt][V], g[kVpt][V];
@@ -451,30 +463,44 @@ __global__ void __launch_bounds__(kThreads) layer_norm_dx_wide_kernel(LayerNormG
   const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
   T* dx = static_cast<T*>(a.dx) + row * a.lddx;
   const float m = a.mean[row], rs = a.rstd[row];
-  float c1 = 0.f, c2 = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int64_t vec = threadIdx.x; vec < nvec_warp; vec += kThreads) {
-      float xv[V], g[V], w[V];
-      Elem<T>::unpack(load_one(x, W, vec), xv);
-      Elem<T>::unpack(load_one(dy, W, vec), g);
-      if (a.weight) load_f32<TW, V>(static_cast<const TW*>(a.weight), W, vec, w);
+  // xhat and g = dy w of a vector
+  auto read = [&](int64_t vec, float (&xh)[V], float (&g)[V]) {
+    float w[V];
+    Elem<T>::unpack(load_one(x, W, vec), xh);
+    Elem<T>::unpack(load_one(dy, W, vec), g);
+    if (a.weight) load_f32<TW, V>(static_cast<const TW*>(a.weight), W, vec, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (xv[e] - m) * rs;
-        if (a.weight) g[e] *= w[e];
-        if (pass == 0) {
-          c1 += g[e];
-          c2 += g[e] * xh;
-        } else {
-          g[e] = rs * (g[e] - c1 - xh * c2);
-        }
+    for (int e = 0; e < V; ++e) {
+      xh[e] = (xh[e] - m) * rs;
+      if (a.weight) g[e] *= w[e];
+    }
+  };
+  float c1 = 0.f, c2 = 0.f, xh[V], g[V];
+  for (int64_t vec = threadIdx.x; (vec + 1) * V <= W; vec += kThreads) {
+    read(vec, xh, g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      c1 += g[e];
+      c2 += g[e] * xh[e];
+    }
+  }
+  if (W % V != 0 && threadIdx.x == W / V % kThreads) {  // the row's last, partial vector
+    read(W / V, xh, g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (e < W % V) {
+        c1 += g[e];
+        c2 += g[e] * xh[e];
       }
-      if (pass == 1) store_vec(dx, W, vec, Elem<T>::pack(g));
     }
-    if (pass == 0) {
-      c1 = row_sum<kThreads>(c1, buf[0]) / static_cast<float>(W);
-      c2 = row_sum<kThreads>(c2, buf[1]) / static_cast<float>(W);
-    }
+  }
+  c1 = row_sum<kThreads>(c1, buf[0]) / static_cast<float>(W);
+  c2 = row_sum<kThreads>(c2, buf[1]) / static_cast<float>(W);
+  for (int64_t vec = threadIdx.x; vec < nvec_warp; vec += kThreads) {
+    read(vec, xh, g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) g[e] = rs * (g[e] - c1 - xh[e] * c2);
+    store_vec(dx, W, vec, Elem<T>::pack(g));
   }
 }
 
