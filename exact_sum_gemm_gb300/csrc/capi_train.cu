@@ -53,12 +53,23 @@ det_status check_shape(det_dtype dtype, const det_attention_shape* s) {
   if (s->batch < 0 || s->lq < 0 || s->lk < 0 || s->hq < 1 || s->hkv < 1 || s->dim < 1) return DET_ERR_SHAPE;
   if (s->batch > kMax || s->lq > kMax || s->lk > kMax || s->hq > 65535 || s->hkv > s->hq) return DET_ERR_SHAPE;
   if (s->hq % s->hkv != 0 || s->dim > DET_MAX_HEAD_DIM) return DET_ERR_SHAPE;
-  // a block per 64 rows of each head of each entry, and per eight rows once
+  // blocks of a launch, for each head of each entry: one per 64 rows, or per 16 (the f32 split), at most
   const int64_t tiles = (s->lq > s->lk ? s->lq : s->lk) / 8 + 1;
   if (s->batch > 0 && tiles > kMaxRows / (s->batch * s->hq)) return DET_ERR_SHAPE;
   if ((s->causal != 0 && s->causal != 1) || !isfinite(s->scale)) return DET_ERR_INVALID_ARG;
   if (s->k_lengths != nullptr && !aligned(s->k_lengths, 4)) return DET_ERR_ALIGNMENT;
   return DET_OK;
+}
+
+// Of a shape that check_shape passes.  Backward has a block per 64 queries (dq)
+// and per 64 keys (dk and dv) in one launch, and, bf16, one per 16 queries, of
+// which a head has whole 128s.
+det_status check_backward_blocks(det_dtype dtype, const det_attention_shape* s, bool dq, bool dkv) {
+  int64_t tiles = 0;
+  if (dq) tiles += s->batch * s->hq * ((s->lq + 63) / 64);
+  if (dkv) tiles += s->batch * s->hkv * ((s->lk + 63) / 64);
+  const int64_t statistics = dtype == DET_BF16 ? s->batch * s->hq * ((s->lq + 127) / 128 * 8) : 0;
+  return tiles > kMaxRows || statistics > kMaxRows ? DET_ERR_SHAPE : DET_OK;
 }
 
 // `elements`: of the tensor; an empty one is never touched.
@@ -182,6 +193,7 @@ det_status det_attention_backward(det_dtype dtype, const det_attention_shape* sh
                                   const float* lse, det_heads dq, det_heads dk, det_heads dv,
                                   void* stream) {
   DET_CHECK(check_shape(dtype, shape));
+  DET_CHECK(check_backward_blocks(dtype, shape, dq.ptr != nullptr, dk.ptr != nullptr));
   const int64_t nq = shape->batch * shape->lq, nk = shape->batch * shape->lk;
   DET_CHECK(check_heads(dout, dtype, nq));
   DET_CHECK(check_heads(q, dtype, nq));

@@ -89,8 +89,9 @@ struct AttentionArgs {
   Heads dout, dq, dk, dv;      // backward; dq.p / dk.p null: not wanted
   float* lse;              // [batch, hq, lq]: written by forward, read by backward
   // Scratch of backward, [batch, hq, stat_stride] with stat_stride = lq rounded
-  // up to 64: sum_d do o (0 past lq), and lse log2(e) (+inf for a query without
-  // a key and past lq: its probabilities are then 0).
+  // up to 128, as the kernels copy whole steps of up to 128 rows: sum_d do o (0
+  // past lq), and lse log2(e) (+inf for a query without a key and past lq: its
+  // probabilities are then 0).
   float* delta;
   float* lse2;
   int64_t stat_stride;
