@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(LogprobsGra
 
 constexpr int64_t kResident = kBlocksPerSm * 152;                  // blocks that a GB300 holds at once
 constexpr int64_t kSplitBelow = 2 * kResident;
-constexpr int64_t kMaxGridY = 32768;
+constexpr int64_t kMaxGridY = 65535;                               // (y times z: more rows than there can be)
 
 template <typename T, bool kTop, bool kPlain>
 cudaError_t launch_forward(const LogprobsArgs& a, int segments, int per, int splits, cudaStream_t stream) {
