@@ -30,9 +30,9 @@ def check(x, w, b, dy, eps=1e-5):
     return got
 
 
-# widths on both sides of every kernel's limit: a warp per row up to 128
-# vectors (512 f32, 1024 bf16), a block up to 16384 elements backward and 4096
-# vectors forward, then the re-reading kernels; odd ones start rows off 16 bytes
+# widths on both sides of every kernel's limit: a warp per row up to 512
+# columns, a block up to 16384, then the re-reading kernels; odd ones start rows
+# off 16 bytes
 @pytest.mark.parametrize("width", [1, 2, 3, 7, 8, 31, 64, 127, 128, 129, 256, 257, 511, 512, 513,
                                    1000, 1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 5001, 8192,
                                    8193, 16383, 16384, 16385, 32768, 32771])
