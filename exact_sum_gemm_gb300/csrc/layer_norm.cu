@@ -19,10 +19,13 @@
 // ahead.  Measured, of the copy bandwidth of 6.69 TB/s: f32 16384 x 4096 forward
 // 79 us (6.8 TB/s), backward 115 + 6 us (7.0 TB/s; the 6 are the reduction of
 // dw and db over the blocks); bf16 8192 x 4096 27 us (5.0 TB/s) and 42 + 6 us
-// (4.8 TB/s).  bf16 has half the time for the same instructions and is bound by
-// their issue (68 % of the slots forward, a block's two barriers a row being the
-// rest); so are rows that do not start on 16 bytes, whose vectors are shifted
-// into place: 1111 x 5001 17 us.
+// (4.8 TB/s).  bf16 has half the time for the same instructions: forward they
+// take 71 % of the issue slots, a block's two barriers a row being part of the
+// rest.  Backward is bound by latency: 16 warps of 128 registers to an SM (22 %),
+// 57 % of the issue slots, one barrier a row.  So are rows that do not start on
+// 16 bytes (bf16 1111 x 5001 forward 17 us: 51 % of the slots, 8 % of DRAM): their
+// vectors are loaded to registers, shifted into place and stored to the ring, so
+// that a row to come is waited for before the present one is summed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -562,7 +565,13 @@ __global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const float* pa
 // of the sums over rows does not depend on the device.
 constexpr int64_t kSms = 152;
 // Up to this many rows the backward pass is one launch that reads x and dy
-// twice.
+// twice: 64 rows of 1024, 4096, 16384 columns take 3.5, 4.2, 7.0 us (f32) and
+// 3.8, 4.4, 8.1 us (bf16), where 65 take the persistent blocks and the reduction
+// 4.8, 7.3, 20.8 us and 5.4, 9.2, 28.5 us.  A call that wants dx alone takes the
+// same launch at any number of rows, for its blocks of one row: faster than the
+// persistent blocks with their sums at 1000 x 1024 (f32 5.2 us for 10.2, bf16 4.5
+// for 12.4) and slower where the ring pays, f32 8192 x 4096 78 us for 51, bf16 64
+// for 45.  (A form of the persistent blocks without sums is not there.)
 constexpr int64_t kFewRows = 64;
 
 // More than 48 KB of shared memory, static included, has to be asked for once
