@@ -363,12 +363,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ref = next;
       }
       const float sub = ref == -INFINITY ? 0.f : ref;
+      float by_c = c;
+      if (__any_sync(0xFFFFFFFFu, fabsf(sub) >= kFar)) {
+#pragma unroll
+        for (int cb = 0; cb < kKeys / 32; ++cb) scale_far(v[cb], sub, c);
+        if (fabsf(sub) >= kFar) by_c = 1.f;
+      }
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int cb = 0; cb < kKeys / 32; ++cb) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          float p = exp2_approx(fmaf(__uint_as_float(v[cb][e]), c, -sub));
+          float p = exp2_approx(fmaf(__uint_as_float(v[cb][e]), by_c, -sub));
           if (c == 0.f && !whole && 32 * cb + e >= seen) p = 0.f;       // (0 x inf)
           sum[e & 3] += p;
           v[cb][e] = __float_as_uint(p);

@@ -428,6 +428,18 @@ __device__ __forceinline__ void hide(uint32_t (&v)[32], int seen, float scale) {
     if (e >= seen) v[e] = hidden;
 }
 
+// 2^(s c - ref) is taken with one rounding, ref being the rounded s c of some s.
+// Its rounding is a factor of all of a row's exponentials, which cancels while it
+// is small: below kFar at most 2^(2^-11), so that the largest probability is 1
+// rounded to bf16 too; from 2^30 on they would overflow.  Further away the scores
+// are multiplied and rounded as ref was.
+constexpr float kFar = 8192.f;
+__device__ __forceinline__ void scale_far(uint32_t (&v)[32], float ref, float c) {
+  const float by = fabsf(ref) >= kFar ? c : 1.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), by));
+}
+
 // Maximum (minimum) of a row's scores; NaN if one is.
 template <bool kMin>
 __device__ __forceinline__ float row_extreme(const uint32_t (&v)[2][32]) {

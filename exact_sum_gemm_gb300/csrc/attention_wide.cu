@@ -175,12 +175,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ref = top;
       }
       const float sub = ref == -INFINITY ? 0.f : ref;
+      float by_c = c;
+      if (__any_sync(0xFFFFFFFFu, fabsf(sub) >= kFar)) {
+        scale_far(v, sub, c);
+        if (fabsf(sub) >= kFar) by_c = 1.f;
+      }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t x[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float p = exp2_approx(fmaf(__uint_as_float(v[16 * g + e]), c, -sub));
+          float p = exp2_approx(fmaf(__uint_as_float(v[16 * g + e]), by_c, -sub));
           if (!whole && 16 * g + e >= seen) p = 0.f;
           l += p;
           x[e] = __float_as_uint(p);
