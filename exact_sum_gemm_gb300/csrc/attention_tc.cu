@@ -865,7 +865,7 @@ __device__ __forceinline__ void backward_block(const AttentionArgs& a, unsigned*
           }
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const float p = exp2_approx(fmaf(__uint_as_float(sv[e + f]), c, -l[f]));
+            const float p = probability(fmaf(__uint_as_float(sv[e + f]), c, -l[f]));
             dv[e + f] = __float_as_uint(p * (__uint_as_float(dv[e + f]) - d[f]));
             sv[e + f] = __float_as_uint(p);
           }
@@ -910,7 +910,7 @@ __device__ __forceinline__ void backward_block(const AttentionArgs& a, unsigned*
             const float by[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int f = 0; f < 4; ++f)
-              p[h][e + f] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(p[h][e + f]), c, -by[f])));
+              p[h][e + f] = __float_as_uint(probability(fmaf(__uint_as_float(p[h][e + f]), c, -by[f])));
           }
           hide(p[h], 32 * h);
           put_pairs(p[h], at + 16 * h);
@@ -945,7 +945,7 @@ __device__ __forceinline__ void backward_block(const AttentionArgs& a, unsigned*
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            sv[e] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(sv[e]), c, -own_lse)));
+            sv[e] = __float_as_uint(probability(fmaf(__uint_as_float(sv[e]), c, -own_lse)));
           if (c0 == 0) {
             if (!wait_warp(&bars.dp_full, i & 1)) return false;
             ptx::tc_fence_after();

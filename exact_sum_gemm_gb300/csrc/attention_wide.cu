@@ -423,7 +423,7 @@ __device__ __forceinline__ void wide_block(const AttentionArgs& a, unsigned* sta
       if (upper) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float x = exp2_approx(fmaf(__uint_as_float(v[e]), c, kKeysHome ? -stat[e] : -own_lse));
+          float x = probability(fmaf(__uint_as_float(v[e]), c, kKeysHome ? -stat[e] : -own_lse));
           if (e < lo || e >= hi) x = 0.f;
           p[e][home] = x;
           v[e] = __float_as_uint(x);

@@ -268,10 +268,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Maximum that keeps a NaN.
+// Maximum and minimum that keep a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float warp_max_nan(float v) {
@@ -286,6 +291,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// A probability from its binary logarithm, which is at most 0 but for the
+// rounding of what it is the difference of.
+__device__ __forceinline__ float probability(float x) { return exp2_approx(min_nan(x, 0.f)); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 

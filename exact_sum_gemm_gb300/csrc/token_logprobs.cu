@@ -360,11 +360,6 @@ __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, co
 }
 
 // Largest and smallest of a vector's elements, NaN if one is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -437,6 +437,8 @@ det_status det_attention_forward(det_dtype dtype, const det_attention_shape* sha
  * k, v, o and lse; the probabilities are recomputed.  dq.ptr null: not wanted;
  * dk.ptr and dv.ptr both null: not wanted.  Gradients of shared key heads are
  * summed over their query heads; hidden keys and queries without a key get 0.
+ * The relative error of a recomputed probability grows with the scores, by about
+ * 2^-22 per unit of the largest; it is never above 1.
  */
 det_status det_attention_backward(det_dtype dtype, const det_attention_shape* shape, det_heads dout,
                                   det_heads q, det_heads k, det_heads v, det_heads o,

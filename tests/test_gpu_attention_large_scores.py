@@ -52,3 +52,28 @@ def test_forward(size, scale, dim, lq, lk, dt):
     # the negative scores: the smallest product takes all
     o2, _ = dg.det_attention_forward(q, -k, v, scale=-scale)
     assert torch.equal(o2, o)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dim,lq,lk", [(64, 40, 300), (64, 300, 300), (128, 300, 300), (96, 130, 70), (128, 33, 50)])
+@pytest.mark.parametrize("size", SIZES)
+def test_backward(size, dim, lq, lk, dt):
+    """No probability above 1: dv is at most the sum of |do| of the queries, whatever the scores' rounding."""
+    q, k, v, do, best, top = one_hot_scores(lq, lk, dim, size, dt, seed=1)
+    most = torch.zeros(lk, dim, dtype=torch.float64, device="cuda")
+    most.index_add_(0, best, do[0, :, 0].double().abs())
+    want = torch.zeros(lk, dim, dtype=torch.float64, device="cuda")
+    want.index_add_(0, best, do[0, :, 0].double())
+    for i in range(8):
+        scale = 0.3 + 0.037 * i
+        o, lse = dg.det_attention_forward(q, k, v, scale=scale)
+        dq, dk, dv = dg.det_attention_backward(do, q, k, v, o, lse, scale=scale)
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            assert t.isfinite().all(), (name, scale)
+        others = 16 * lq * math.exp(-size * scale / 8) * 6
+        assert (dv[0, :, 0].double().abs() <= most * (1 + 2.0 ** -7) + others).all(), scale
+        # while the rounding of the scores is small, the gradient itself: six roundings of 2 size * scale in
+        # the exponent
+        if size <= 2.0 ** 14:
+            off = 12 * U * size * scale + (2.0 ** -7 if dt == BF16 else 2.0 ** -20)
+            assert ((dv[0, :, 0].double() - want).abs() <= off * most + others).all(), scale
