@@ -14,10 +14,12 @@ det_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DET_OK : DET_ERR
 bool dtype_ok(det_dtype t) { return t == DET_F32 || t == DET_BF16; }
 uintptr_t size_of(det_dtype t) { return t == DET_F32 ? 4 : 2; }
 
-// One block per row, and byte offsets that stay within 63 bits.
+// One block per row, and byte offsets that stay within 63 bits: no axis reaches
+// over more than 2^58 elements.
 constexpr int64_t kMaxRows = 0x7FFFFFFFll;
 constexpr int64_t kMaxWidth = 0x7FFFFFFFll - 0xFFFF;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+bool reaches_too_far(int64_t n, int64_t stride) { return n > 1 && stride > (int64_t(1) << 58) / n; }
 
 det_status check_rows(det_dtype dtype, int64_t rows, int64_t width) {
   if (!dtype_ok(dtype)) return DET_ERR_DTYPE;
@@ -26,8 +28,8 @@ det_status check_rows(det_dtype dtype, int64_t rows, int64_t width) {
 }
 
 // A row-wise operand that is read or written.
-det_status check_operand(const void* p, int64_t ld, int64_t width, uintptr_t size) {
-  if (p == nullptr || ld < width || ld > kMaxStride) return DET_ERR_INVALID_ARG;
+det_status check_operand(const void* p, int64_t rows, int64_t ld, int64_t width, uintptr_t size) {
+  if (p == nullptr || ld < width || ld > kMaxStride || reaches_too_far(rows, ld)) return DET_ERR_INVALID_ARG;
   return aligned(p, size) ? DET_OK : DET_ERR_ALIGNMENT;
 }
 det_status check_vector(const void* p, uintptr_t size) {
@@ -72,12 +74,15 @@ det_status check_backward_blocks(det_dtype dtype, const det_attention_shape* s, 
   return tiles > kMaxRows || statistics > kMaxRows ? DET_ERR_SHAPE : DET_OK;
 }
 
-// `elements`: of the tensor; an empty one is never touched.
-det_status check_heads(const det_heads& h, det_dtype dtype, int64_t elements) {
-  if (elements == 0) return DET_OK;
+// A tensor of `length` rows of `heads` heads; an empty one is never touched.
+det_status check_heads(const det_heads& h, det_dtype dtype, int64_t batch, int64_t length, int64_t heads) {
+  if (batch == 0 || length == 0) return DET_OK;
   if (h.ptr == nullptr) return DET_ERR_INVALID_ARG;
   for (int64_t s : {h.stride_batch, h.stride_length, h.stride_head})
     if (s < 0 || s > kMaxStride) return DET_ERR_INVALID_ARG;
+  if (reaches_too_far(batch, h.stride_batch) || reaches_too_far(length, h.stride_length) ||
+      reaches_too_far(heads, h.stride_head))
+    return DET_ERR_INVALID_ARG;
   return aligned(h.ptr, size_of(dtype)) ? DET_OK : DET_ERR_ALIGNMENT;
 }
 
@@ -115,8 +120,8 @@ det_status det_layer_norm_forward(det_dtype dtype, det_dtype weight_dtype, int64
   DET_CHECK(check_rows(dtype, rows, width));
   if (!(eps >= 0.f) || !isfinite(eps)) return DET_ERR_INVALID_ARG;
   if (rows == 0 || width == 0) return DET_OK;
-  DET_CHECK(check_operand(x, ldx, width, size_of(dtype)));
-  DET_CHECK(check_operand(y, ldy, width, size_of(dtype)));
+  DET_CHECK(check_operand(x, rows, ldx, width, size_of(dtype)));
+  DET_CHECK(check_operand(y, rows, ldy, width, size_of(dtype)));
   DET_CHECK(check_vector(mean, 4));
   DET_CHECK(check_vector(rstd, 4));
   if (!aligned(weight, size_of(weight_dtype)) || !aligned(bias, size_of(weight_dtype))) return DET_ERR_ALIGNMENT;
@@ -148,9 +153,9 @@ det_status det_layer_norm_backward(det_dtype dtype, det_dtype weight_dtype, int6
     if (!aligned(p, size_of(weight_dtype))) return DET_ERR_ALIGNMENT;
   if (width == 0) return DET_OK;
   if (rows > 0) {
-    DET_CHECK(check_operand(dy, lddy, width, size_of(dtype)));
-    DET_CHECK(check_operand(x, ldx, width, size_of(dtype)));
-    if (dx != nullptr) DET_CHECK(check_operand(dx, lddx, width, size_of(dtype)));
+    DET_CHECK(check_operand(dy, rows, lddy, width, size_of(dtype)));
+    DET_CHECK(check_operand(x, rows, ldx, width, size_of(dtype)));
+    if (dx != nullptr) DET_CHECK(check_operand(dx, rows, lddx, width, size_of(dtype)));
     DET_CHECK(check_vector(mean, 4));
     DET_CHECK(check_vector(rstd, 4));
   }
@@ -176,12 +181,13 @@ det_status det_layer_norm_backward(det_dtype dtype, det_dtype weight_dtype, int6
 det_status det_attention_forward(det_dtype dtype, const det_attention_shape* shape, det_heads q,
                                  det_heads k, det_heads v, det_heads o, float* lse, void* stream) {
   DET_CHECK(check_shape(dtype, shape));
-  const int64_t nq = shape->batch * shape->lq, nk = shape->batch * shape->lk;
-  DET_CHECK(check_heads(q, dtype, nq));
-  DET_CHECK(check_heads(k, dtype, nk));
-  DET_CHECK(check_heads(v, dtype, nk));
-  DET_CHECK(check_heads(o, dtype, nq));
-  if (nq == 0) return DET_OK;
+  const auto check_queries = [&](const det_heads& h) { return check_heads(h, dtype, shape->batch, shape->lq, shape->hq); };
+  const auto check_keys = [&](const det_heads& h) { return check_heads(h, dtype, shape->batch, shape->lk, shape->hkv); };
+  DET_CHECK(check_queries(q));
+  DET_CHECK(check_keys(k));
+  DET_CHECK(check_keys(v));
+  DET_CHECK(check_queries(o));
+  if (shape->batch == 0 || shape->lq == 0) return DET_OK;
   DET_CHECK(check_vector(lse, 4));
   det::AttentionArgs a = attention_args(dtype, shape, q, k, v, o);
   a.lse = lse;
@@ -194,18 +200,19 @@ det_status det_attention_backward(det_dtype dtype, const det_attention_shape* sh
                                   void* stream) {
   DET_CHECK(check_shape(dtype, shape));
   DET_CHECK(check_backward_blocks(dtype, shape, dq.ptr != nullptr, dk.ptr != nullptr));
-  const int64_t nq = shape->batch * shape->lq, nk = shape->batch * shape->lk;
-  DET_CHECK(check_heads(dout, dtype, nq));
-  DET_CHECK(check_heads(q, dtype, nq));
-  DET_CHECK(check_heads(k, dtype, nk));
-  DET_CHECK(check_heads(v, dtype, nk));
-  DET_CHECK(check_heads(o, dtype, nq));
-  if (nq > 0) DET_CHECK(check_vector(lse, 4));
-  if (dq.ptr != nullptr) DET_CHECK(check_heads(dq, dtype, nq));
+  const auto check_queries = [&](const det_heads& h) { return check_heads(h, dtype, shape->batch, shape->lq, shape->hq); };
+  const auto check_keys = [&](const det_heads& h) { return check_heads(h, dtype, shape->batch, shape->lk, shape->hkv); };
+  DET_CHECK(check_queries(dout));
+  DET_CHECK(check_queries(q));
+  DET_CHECK(check_keys(k));
+  DET_CHECK(check_keys(v));
+  DET_CHECK(check_queries(o));
+  if (shape->batch > 0 && shape->lq > 0) DET_CHECK(check_vector(lse, 4));
+  if (dq.ptr != nullptr) DET_CHECK(check_queries(dq));
   if ((dk.ptr == nullptr) != (dv.ptr == nullptr)) return DET_ERR_INVALID_ARG;
   if (dk.ptr != nullptr) {
-    DET_CHECK(check_heads(dk, dtype, nk));
-    DET_CHECK(check_heads(dv, dtype, nk));
+    DET_CHECK(check_keys(dk));
+    DET_CHECK(check_keys(dv));
   }
   det::AttentionArgs a = attention_args(dtype, shape, q, k, v, o);
   a.dout = heads(dout);
@@ -223,7 +230,7 @@ det_status det_token_logprobs_forward(det_dtype dtype, int64_t rows, int64_t voc
   DET_CHECK(check_rows(dtype, rows, vocab));
   if (vocab < 1 || top < 0 || top > DET_MAX_TOP || top > vocab) return DET_ERR_SHAPE;
   if (rows == 0) return DET_OK;
-  DET_CHECK(check_operand(logits, ld, vocab, size_of(dtype)));
+  DET_CHECK(check_operand(logits, rows, ld, vocab, size_of(dtype)));
   DET_CHECK(check_vector(tokens, 8));
   DET_CHECK(check_vector(logprobs, 4));
   DET_CHECK(check_vector(entropy, 4));
@@ -256,8 +263,8 @@ det_status det_token_logprobs_backward(det_dtype dtype, int64_t rows, int64_t vo
   DET_CHECK(check_rows(dtype, rows, vocab));
   if (vocab < 1) return DET_ERR_SHAPE;
   if (rows == 0) return DET_OK;
-  DET_CHECK(check_operand(logits, ld, vocab, size_of(dtype)));
-  DET_CHECK(check_operand(dlogits, ldd, vocab, size_of(dtype)));
+  DET_CHECK(check_operand(logits, rows, ld, vocab, size_of(dtype)));
+  DET_CHECK(check_operand(dlogits, rows, ldd, vocab, size_of(dtype)));
   DET_CHECK(check_vector(tokens, 8));
   DET_CHECK(check_vector(entropy, 4));
   DET_CHECK(check_vector(stats, 4));
