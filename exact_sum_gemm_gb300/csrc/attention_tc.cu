@@ -62,14 +62,14 @@
 // the products of the other running.
 //
 // bf16, 2 x 4096 causal, 16/4 heads of 128: forward 142 us (968 TFLOP/s of the
-// visible pairs' products), backward 390 us (881 counting five products, 1234
+// visible pairs' products), backward 392 us (877 counting five products, 1228
 // counting the seven; a plain product reaches 1867).  Whole tiles along the
 // diagonal come on top.  The tensor pipe is busy for 41 and 53 % of the cycles,
-// the issue slots are for 49 and 33 %: neither is at its limit.  What is left is
-// the chain of a step (products, TMEM read, exponentials, TMEM write, products),
-// in forward also the start and end of a block (an eighth of its time).  f32
-// 2 x 1024, 8 heads of 64: split 7, forward 32, split with statistics 8, backward
-// 68 us, six times the products of bf16.
+// the issue slots are for 49 and 33 %: neither is at its limit.  What is left of
+// backward is the chain of a step (products, TMEM read, exponentials, TMEM write,
+// products); forward's waits have not been measured, the start and end of a block
+// are an eighth of its time.  f32 2 x 1024, 8 heads of 64: split 7, forward 33,
+// split with statistics 8, backward 68 us, six times the products of bf16.
 //
 // Every wait is bounded (about 2 s); where one runs out the outputs are NaN and
 // the library's device status records it.
